@@ -314,3 +314,33 @@ def test_graph_replay_on_another_stream():
         check_forward(out, nx, nr, gamma.cpu())
         check_backward(dx, dg, out[0].cpu(), gamma.cpu(), out[1].cpu(), nx)
     assert m.moe_get_last_error() == 0
+
+
+@pytest.mark.parametrize("T,H", [(2048, 4096), (300, 4096), (1500, 4097), (64, 65536), (64, 65537)])
+def test_codes_are_the_rounded_quotients(T, H):
+    # fp32 rows: y as stored is what is quantised, so a code is y / q_scale, rounded to fp32 and
+    # then to e4m3, and nothing else
+    m = G.lib()
+    x, _, gamma = inputs(T, H, torch.float32, False, seed=6)
+    _, y, q, s = forward(m.make_norm(T, H, torch.float32), x, None, gamma, h=False)
+    want = (y.cpu() / s.cpu()[:, None]).to(E4M3)
+    off = (q.cpu().view(torch.uint8) != want.view(torch.uint8)).sum().item()
+    assert off == 0, f"{off} of {T * H} codes differ"
+
+
+@pytest.mark.parametrize("T,H", [(60, 512), (700, 512), (60, 509)])
+def test_codes_at_the_midpoints(T, H):
+    # rows of the midpoints between neighbouring codes, both signs, with 448 as the largest: every
+    # quotient is a tie or a rounding away from one
+    m = G.lib()
+    codes = torch.arange(127, dtype=torch.uint8).view(E4M3).float()
+    mid = (codes[1:] + codes[:-1]) / 2
+    g = gen(8)
+    x = mid[torch.randint(0, 126, (T, H), generator=g)] * (torch.randint(0, 2, (T, H), generator=g) * 2 - 1)
+    x[:, 7] = 448.0
+    x *= torch.exp2(torch.randint(-20, 20, (T, 1), generator=g).float())
+    gamma = torch.full((H,), 1.25)
+    _, y, q, s = forward(m.make_norm(T, H, torch.float32), x, None, gamma, h=False)
+    want = (y.cpu() / s.cpu()[:, None]).to(E4M3)
+    off = (q.cpu().view(torch.uint8) != want.view(torch.uint8)).sum().item()
+    assert off == 0, f"{off} of {T * H} codes differ"
