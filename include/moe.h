@@ -469,7 +469,7 @@ size_t moe_norm_workspace_bytes(const moe_norm* n);
 /* The residual's addition, the root-mean-square norm and the per-row fp8
  * quantisation in front of the layer, in one pass:
  *   h = x + residual (x alone without one);  m = 1 / sqrt(mean(h^2) + eps)
- *   y = h * m * gamma;  q_scale = max|y| / 448 (1 for a row of zeros)
+ *   y = h * m * gamma;  q_scale = max|y| / 448 (1 where that rounds to zero)
  *   q = e4m3(y / q_scale), nearest even
  * y and q are taken from the fp32 sum, each rounded once, and h is its rounding.
  * (Kimi K3 report, s.2.4 RMSNorm; Ling write-up, s.5 activation quantisation: q

@@ -2,7 +2,7 @@
 // the layer, with rows quantised for the experts, and the gradient.
 //
 //   h = x + r;  m = rsqrt(mean(h^2) + eps);  y = h m gamma
-//   s = max|y| / 448 (1 for a row of zeros);  q = e4m3(y / s)
+//   s = max|y| / 448 (1 where that is zero);  q = e4m3(y / s)
 // with u = gamma dy and dh the gradient that arrives on h itself:
 //   dx = dr = m u - h m^3 mean(u h) + dh
 //   dgamma = sum_t dy_t h_t m_t
@@ -58,9 +58,11 @@ __device__ __forceinline__ float block_max(float v, float* s_red) {
   return v;
 }
 
-// Scale of a quantised row: 1 for a row of zeros; a NaN stays one.
+// Scale of a quantised row: 1 for a row of zeros, and for one whose scale rounds to
+// zero; a NaN stays one.
 __device__ __forceinline__ float row_scale(float amax) {
-  return amax == 0.0f ? 1.0f : amax / 448.0f;
+  const float s = amax / 448.0f;
+  return s == 0.0f ? 1.0f : s;
 }
 
 // y / s as near as e4m3's rounding needs it: z has the code of the quotient rounded to

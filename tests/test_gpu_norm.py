@@ -344,3 +344,22 @@ def test_codes_at_the_midpoints(T, H):
     want = (y.cpu() / s.cpu()[:, None]).to(E4M3)
     off = (q.cpu().view(torch.uint8) != want.view(torch.uint8)).sum().item()
     assert off == 0, f"{off} of {T * H} codes differ"
+
+
+@pytest.mark.parametrize("H", [256, 257, 16389])
+def test_scales_below_the_smallest_number(H):
+    # a row whose largest |y| is so small that |y| / 448 rounds to zero is a row of zeros in
+    # eight bits: scale 1, as for zeros themselves; a scale of a few of the smallest numbers stays
+    m = G.lib()
+    x = torch.ones(4, H)
+    x[0] = 0.0
+    x[2, 1:] = 0.0  # m = sqrt(H)
+    gamma = torch.full((H,), 1e-44)
+    n = m.make_norm(4, H, torch.float32)
+    _, y, q, s = (None if v is None else v.cpu() for v in forward(n, x, None, gamma, h=False))
+    assert y[1].ne(0).all() and s[:2].eq(1.0).all() and s[3] == 1.0
+    assert not q[:2].float().any() and not q[3].float().any()
+    gamma = torch.full((H,), 1e-42)
+    _, y, q, s = (v.cpu() for v in forward(n, x, None, gamma))
+    assert s[0] == 1.0 and 0.0 < s[1] < 1e-44 and not q[0].float().any()
+    assert torch.equal(q[1:].view(torch.uint8), (y[1:] / s[1:, None]).clamp(max=448.0).to(E4M3).view(torch.uint8))
