@@ -52,7 +52,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
     const float x = expf(-fabsf(l)), r = 1.0f / (1.0f + x);
     const float score = e >= 0 ? (l >= 0.0f ? r : x * r) : 0.0f;
     const float total = warp_sum(score);
-    d = total > 0.0f ? x * r * r * d / total : 0.0f;
+    // a NaN stays one; scores that have all underflowed have no gradient
+    d = total == 0.0f ? 0.0f : x * r * r * d / total;
   } else {
     d *= wj;
   }

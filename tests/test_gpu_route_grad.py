@@ -116,3 +116,41 @@ def test_empty_batch():
     m.moe_route_backward(problem(0, 8, 2, False), None, torch.empty(0, 2, dtype=torch.int32, device="cuda"),
                          e(0, 2), e(0, 2), e(0, 8))
     assert m.moe_get_last_error() == 0
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+def test_nan_of_a_chosen_logit_stays(sigmoid):
+    # the weights of its token have no gradient, which must show; other tokens, masked slots
+    # and logits that were not chosen are as without it
+    T, E, k = 12, 10, 3
+    g = torch.Generator().manual_seed(4)
+    idx = B.routing(T, E, k, g)
+    idx[5, 2] = -1
+    logits = torch.randn(T, E, generator=g)
+    w, dw = B.route_weights(logits, idx, sigmoid).float(), torch.randn(T, k, generator=g)
+    p = problem(T, E, k, sigmoid)
+    want = backward(p, logits, idx, w, dw).cpu()
+    chosen = idx.clamp(min=0).long()
+    bad = logits.clone()
+    for t in (0, 5):
+        bad[t, chosen[t, 1]] = float("nan")
+    other = next(e for e in range(E) if e not in chosen[7].tolist())
+    bad[7, other] = float("nan")  # not chosen
+    w = B.route_weights(bad, idx, sigmoid).float()
+    out = backward(p, bad, idx, w, dw).cpu()
+    assert G.lib().moe_get_last_error() == 0
+    keep = [t for t in range(T) if t not in (0, 5)]
+    assert torch.equal(out[keep], want[keep])
+    for t in (0, 5):
+        live = torch.zeros(E, dtype=torch.bool)
+        live[chosen[t][idx[t] >= 0]] = True
+        assert out[t, live].isnan().all() and not out[t, ~live].any()
+
+
+def test_scores_that_underflow_have_no_gradient():
+    # sigmoid(-200) is zero in fp32, all of a token's scores are: zeros, not 0 / 0
+    T, E, k = 3, 8, 2
+    logits = torch.full((T, E), -200.0)
+    idx = torch.tensor([[1, 6]] * T, dtype=torch.int32)
+    w, dw = torch.full((T, k), 0.5), torch.tensor([[1.0, -2.0]] * T)
+    assert not backward(problem(T, E, k, True), logits, idx, w, dw).any()
