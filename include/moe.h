@@ -31,7 +31,7 @@
  *     moe_profile_read.
  *   - The library allocates no device memory on the call path: scratch comes
  *     from the caller's workspace `ws` of `ws_bytes` bytes (moe_workspace_bytes),
- *     256-byte aligned.  Outputs must not alias inputs.
+ *     256-byte aligned.  Outputs must not alias inputs (unless the call says so).
  *   - Return value: a moe_status.  Argument checks happen on the host before any
  *     launch and return MOE_ERR_INVALID_ARG / MOE_ERR_UNSUPPORTED /
  *     MOE_ERR_WORKSPACE with nothing queued; a failed launch returns
@@ -478,7 +478,8 @@ size_t moe_norm_workspace_bytes(const moe_norm* n);
  * every code.  Squares are summed in fp32: a row with elements beyond 1e19 has an
  * infinite mean square, and y = 0.
  *   x [T, H];  residual [T, H] or NULL;  gamma [H], all in n's dtype
- *   h [T, H] (out) or NULL (not stored)
+ *   h [T, H] (out) or NULL (not stored);  h and y may each be the buffer of x or of
+ *     residual itself (the residual stream updated in place), not of one another
  *   y [T, H] (out) or NULL;  q [T, H] e4m3 (out) and q_scale [T] fp32 (out), or
  *   both NULL; at least one of y and q */
 int moe_add_rmsnorm(const moe_norm* n, const void* x, const void* residual, const void* gamma,

@@ -363,3 +363,21 @@ def test_scales_below_the_smallest_number(H):
     _, y, q, s = (v.cpu() for v in forward(n, x, None, gamma))
     assert s[0] == 1.0 and 0.0 < s[1] < 1e-44 and not q[0].float().any()
     assert torch.equal(q[1:].view(torch.uint8), (y[1:] / s[1:, None]).clamp(max=448.0).to(E4M3).view(torch.uint8))
+
+
+@pytest.mark.parametrize("dtype,T,H", [("bf16", 3, 512), ("bf16", 700, 512), ("bf16", 5, 1001), ("f32", 700, 1001),
+                                       ("f32", 4, 33000), ("bf16", 4, 131072), ("f32", 3, 16389), ("f16", 3, 32777)])
+@pytest.mark.parametrize("quant", [False, True])
+def test_in_place(dtype, T, H, quant):
+    # the sum in place of the residual and y in place of x, in every kernel of the forward
+    t, m = B.DTYPES[dtype], G.lib()
+    x, r, gamma = inputs(T, H, t, True, seed=7)
+    n = m.make_norm(T, H, t)
+    want = forward(n, x, r, gamma, q=quant)
+    xd, rd = x.cuda(), r.cuda()
+    q, s = (new(T, H, dtype=E4M3), new(T)) if quant else (None, None)
+    m.moe_add_rmsnorm(n, xd, rd, gamma.cuda(), rd, xd, q, s)
+    assert m.moe_get_last_error() == 0
+    assert torch.equal(rd, want[0]) and torch.equal(xd, want[1])
+    if quant:
+        assert torch.equal(q.view(torch.uint8), want[2].view(torch.uint8)) and torch.equal(s, want[3])
