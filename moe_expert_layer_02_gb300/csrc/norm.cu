@@ -629,7 +629,8 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* r, const void* gamma, 
     auto go = [&](auto kern, int threads, int tpr) {
       const int rows = threads / tpr;
       count_launch();
-      return launch_kernel(kern, dim3((T + rows - 1) / rows), dim3(rows * tpr), 0, s, 1,
+      return launch_kernel(kern, dim3((unsigned)(((int64_t)T + rows - 1) / rows)),
+                           dim3(rows * tpr), 0, s, 1,
                            static_cast<const E*>(x), static_cast<const E*>(r),
                            static_cast<const E*>(gamma), static_cast<E*>(h), static_cast<E*>(y),
                            static_cast<uint8_t*>(q), q_scale, T, H, tpr, eps);
@@ -668,10 +669,11 @@ cudaError_t launch_add_rmsnorm_backward(const void* h, const void* gamma, const 
       auto go = [&](auto nv_, auto stages_) {
         constexpr int nv = decltype(nv_)::value, stages = decltype(stages_)::value;
         const int tpr = round32((n + nv - 1) / nv), groups = 512 / tpr, block = groups * tpr;
-        const int one_step = (T + groups - 1) / groups;
-        const int G_ = std::min(G, one_step), steps = (one_step + G_ - 1) / G_;
+        const int one_step = (int)(((int64_t)T + groups - 1) / groups);
+        const int G_ = std::min(G, one_step);
+        const int64_t steps = ((int64_t)one_step + G_ - 1) / G_;
         // as many stages of the ring as a block has rows
-        size_t smem = (size_t)std::min(stages, steps) * (dh ? 3 : 2) * nv * block * 16;
+        size_t smem = (size_t)std::min<int64_t>(stages, steps) * (dh ? 3 : 2) * nv * block * 16;
         smem = std::max(smem, (size_t)(groups > 1 ? groups + 1 : 1) * H * sizeof(float));
         constexpr int kSmem = 192 * 1024;  // any ring at its widest row
         auto run = [&](auto kern, cudaError_t ready, int cluster, float* sums) {

@@ -381,3 +381,27 @@ def test_in_place(dtype, T, H, quant):
     assert torch.equal(rd, want[0]) and torch.equal(xd, want[1])
     if quant:
         assert torch.equal(q.view(torch.uint8), want[2].view(torch.uint8)) and torch.equal(s, want[3])
+
+
+def test_rows_up_to_the_limit_of_their_count():
+    # T = 2^31 - 1: the grids' and the steps' sizes go past 32 bits on their way
+    T, m, t = 2 ** 31 - 1, G.lib(), torch.bfloat16
+    n = m.make_norm(T, 1, t)
+    at = torch.tensor([0, 1, 2 ** 30, T - 17, T - 16, T - 9, T - 8, T - 2, T - 1], device="cuda")
+    x = torch.full((T, 1), -2.0, dtype=t, device="cuda")
+    x[at] = 3.0
+    y = torch.zeros_like(x)
+    gamma = torch.ones(1, dtype=t, device="cuda")
+    m.moe_add_rmsnorm(n, x, None, gamma, None, y, None, None)
+    assert m.moe_get_last_error() == 0
+    # x / |x|, less 2^-23
+    assert (y[at] == 1.0).all() and int((y == -1.0).sum()) == T - len(at)
+    # rows of one element: m (gamma dy) (1 - (h m)^2), 2^-22 of dy at most, rounds off beside dh
+    dx, dg = torch.zeros_like(x), new(1)
+    ws = new(m.moe_norm_workspace_bytes(n), dtype=torch.uint8)
+    m.moe_add_rmsnorm_backward(n, x, gamma, x, x, dx, dg, ws)
+    assert m.moe_get_last_error() == 0
+    assert torch.equal(dx, x)
+    # dgamma: T terms of about 2, summed over T / 2432 rows by a thread and then over those
+    want = 2.0 * (T - len(at)) + 3.0 * len(at)
+    assert abs(dg.item() - want) <= (T / 2432 + 256 + 24) * B.U * want
