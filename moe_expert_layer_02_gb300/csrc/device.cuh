@@ -248,7 +248,10 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
   return r;
 }
 
+// The aligned barrier wants every warp whole and converged; code that branches by lane
+// before it (a loop's last round, one lane's atomic) need not have brought it together.
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
 }

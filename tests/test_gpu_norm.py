@@ -405,3 +405,19 @@ def test_rows_up_to_the_limit_of_their_count():
     # dgamma: T terms of about 2, summed over T / 2432 rows by a thread and then over those
     want = 2.0 * (T - len(at)) + 3.0 * len(at)
     assert abs(dg.item() - want) <= (T / 2432 + 256 + 24) * B.U * want
+
+
+@pytest.mark.parametrize("T", [2, 3, 5, 8])
+@pytest.mark.parametrize("H", [40, 1000, 7185])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_gradient_of_one_cluster(T, H, dtype):
+    # blocks that add each other's sums of dgamma: the last round of each loop before the
+    # cluster's barrier takes part of a warp only
+    t, m = B.DTYPES[dtype], G.lib()
+    x, h, gamma = inputs(T, H, t, True, seed=9)
+    n = m.make_norm(T, H, t)
+    dx, dg = backward(n, h, gamma, x, x)
+    check_backward(dx, dg, h, gamma, x, x)
+    for _ in range(10):
+        again = backward(n, h, gamma, x, x)
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dg)
