@@ -184,8 +184,13 @@ def _stream(stream):
     if _device is None:
         import torch
         torch.cuda.current_stream()  # sets CUDA up
-        # the address itself: a torch.cuda.Stream around it takes 3 us of every call
-        _stream_of, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        # the address itself: a torch.cuda.Stream around it takes 3 us of every call.  These
+        # two names are torch's own and not public: the public call where one is missing
+        of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        if of is None or device is None:
+            of, device = (lambda _: torch.cuda.current_stream().cuda_stream), (lambda: 0)
+        _stream_of, _device = of, device
     return _stream_of(_device())
 
 

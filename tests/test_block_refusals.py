@@ -159,3 +159,26 @@ def test_binding_checks_types_sizes_and_layout(m):
     with pytest.raises(ValueError):
         m.moe_add_rmsnorm(n, torch.empty(4, 64), None, torch.empty(32), None, torch.empty(4, 64),
                           None, None, stream=0)
+
+
+@pytest.mark.parametrize("missing", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_current_stream_without_the_private_lookup(m, monkeypatch, missing):
+    # every entry point takes the current stream; torch's private names for it may go
+    stream = type("Stream", (), {"cuda_stream": 0x1230})()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: stream)
+    monkeypatch.delattr(torch._C, missing)
+    monkeypatch.setattr(m, "_stream_of", None)
+    monkeypatch.setattr(m, "_device", None)
+    assert m._stream(None) == 0x1230
+    stream.cuda_stream = 0x4560  # looked up at every call
+    assert m._stream(None) == 0x4560
+    assert m._stream(stream) == 0x4560 and m._stream(0x20) == 0x20
+
+
+def test_current_stream_by_the_private_lookup(m, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0x100 + d, raising=False)
+    monkeypatch.setattr(m, "_stream_of", None)
+    monkeypatch.setattr(m, "_device", None)
+    assert m._stream(None) == 0x103
