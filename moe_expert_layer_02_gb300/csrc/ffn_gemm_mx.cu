@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
       uint32_t phase = 0;
       bool issued_any = false;
       const uint32_t sfb = tmem + C::SFB_COL;
-      {
+      if (blockIdx.x < n_tiles) {  // (the tiles' own waits cover the copies)
         const uint64_t one = sf_desc(smem_u32(sf + C::STAGES * C::NA * MX_SF_SLOT));
         tmem_cp_32x128_x4(sfb, one);
         tmem_cp_32x128_x4(sfb + 4, one);
@@ -623,7 +623,7 @@ __global__ void __launch_bounds__(MX_THREADS, 1)
       uint32_t phase = 0;
       bool issued_any = false;
       const uint32_t sfb = tmem + C::SFB_COL;
-      {
+      if (cluster < n_tiles) {  // (the tiles' own waits cover the copies)
         const uint64_t one = sf_desc(smem_u32(sf + C::STAGES * C::SF_STAGE));
         tmem_cp_32x128_x4_pair(sfb, one);
         tmem_cp_32x128_x4_pair(sfb + 4, one);

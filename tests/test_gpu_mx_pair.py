@@ -59,3 +59,17 @@ def test_mx_pair_situ(orc):
     got = forward(cfg, G.pack(cfg, inp))
     ref, _, _, _ = orc.moe_forward(cfg.oracle_problem(), G.host(inp))
     G.assert_close(got, ref, "mxfp4 pair SiTU")
+
+
+@pytest.mark.parametrize("single", [0, 1])
+def test_blocks_without_a_tile(orc, tuning, single):
+    # one token: all but a few blocks have nothing to do and leave at once
+    tuning(mx_1cta=single)
+    cfg = ONE_EXPERT.with_(name="mxfp4_pair_one_token", T=1)
+    inp = G.gpu_inputs(cfg)
+    packed = G.pack(cfg, inp)
+    got = forward(cfg, packed)
+    ref, _, _, _ = orc.moe_forward(cfg.oracle_problem(), G.host(inp))
+    G.assert_close(got, ref, "one token")
+    for _ in range(20):
+        assert (forward(cfg, packed) == got).all()
