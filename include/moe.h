@@ -276,7 +276,8 @@ int moe_pack_weights(const moe_problem* p, const void* w13, const void* w2, cons
  *   h[n] = bf16(silu(g[n]) * u[n]);  s_h = max_n |h[n]| / 448;  hq = e4m3(h / s_h)
  *   y[r,m] = bf16(row_w[r] * (sum_n hq[n] W2_e[m,n]) * s_h * s2_e[m])
  * (Ling write-up, s.5 per-channel direct_scaled_dot; FFN1/FFN2 of s.1.)
- *   offsets   [E+1] int32 (device), offsets[E] = R rows
+ *   offsets   [E+1] int32 (device), offsets[E] <= R: rows from offsets[E] on
+ *          (moe_dispatch's of masked slots) are not run and their y is not written
  *   xq_perm   [R, K] e4m3, xscale_perm [R] fp32, row_w [R] fp32 or NULL (= 1)
  *   fp8:   w13 [E, 2I, K] e4m3, w13_scale [E, 2I] fp32,
  *          w2  [E, K, I] e4m3,  w2_scale  [E, K] fp32
@@ -294,7 +295,7 @@ int moe_pack_weights(const moe_problem* p, const void* w13, const void* w2, cons
  *          block scales; K, I <= 16384.  An fp8 shared expert uses the same
  *          format ([2*I_shared/128, H/128] and [H/128, I_shared/128] scales).
  *   y         [R, K] bf16 (out); K = H (or latent)
- * R is read from p as T*top_k. */
+ * R, the size of the buffers, is read from p as T*top_k. */
 int moe_expert_ffn(const moe_problem* p, const int32_t* offsets, const void* xq_perm,
                    const float* xscale_perm, const float* row_w, const void* w13,
                    const void* w13_scale, const void* w2, const void* w2_scale, void* y,
