@@ -470,3 +470,76 @@ def test_dispatched_codes_match_moe_permute():
     for name, want in (("counts", counts), ("offsets", offsets), ("perm", perm), ("src_row", src),
                        ("x_rows", xq), ("scale_rows", xs)):
         assert torch.equal(out[name], want), name
+
+
+@pytest.mark.parametrize("k", [1, 2, 3, 4])
+@pytest.mark.parametrize("H", [8192, 2880, 8191, 4001])
+@pytest.mark.parametrize("T,dtype", [(200, "bf16"), (200, "f32"), (700, "f16")])
+def test_combine_backward_of_few_slots(T, dtype, H, k):
+    # more tokens than multiprocessors and up to four slots: rows of several steps of a ring of
+    # three stages, in whole vectors and in vectors of their own, with masked slots
+    g, t, m, E = gen(T + H + k), B.DTYPES[dtype], G.lib(), 16
+    idx = B.routing(T, E, k, g, 0.2)
+    _, offsets, perm, _ = B.order(idx, E)
+    rows, dout = torch.randn(T * k, H, generator=g).to(t), torch.randn(T, H, generator=g).to(t)
+    w = torch.rand(T, k, generator=g)
+    rows[int(offsets[E]):] = float("nan")
+    w[perm < 0] = float("nan")
+    drows, dw = new(T * k, H, dtype=t), new(T, k)
+    m.moe_combine_backward(m.make_rows(T, H, E, k, t), dout.cuda(), rows.cuda(), perm.cuda(), offsets.cuda(),
+                           w.cuda(), drows, dw)
+    assert m.moe_get_last_error() == 0
+    ref, rw, mag = B.combine_backward(dout, rows, perm, w)
+    B.within(drows, ref, B.store(t, ref) + B.U * ref.abs(), "drows")
+    B.within(dw, rw, (B.chain(H) + 2) * B.U * mag, "dw")
+
+
+# buffers off 16-byte boundaries: a warp or a block per token, one and several steps of a row,
+# groups of slots, the four-slot form, one launch and more, several blocks of columns
+@pytest.mark.parametrize("T,H,k", [(5, 8193, 9), (19, 1031, 3), (700, 100, 9), (700, 100, 2), (700, 250, 9),
+                                   (700, 1031, 2), (700, 8193, 2), (300, 8193, 9), (5000, 250, 2), (5000, 100, 9)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_misaligned_buffers_in_every_variant(T, H, k, dtype):
+    g, t, m, E = gen(T + H + k), B.DTYPES[dtype], G.lib(), 24
+    idx = B.routing(T, E, k, g, 0.2)
+    _, offsets, perm, src = B.order(idx, E)
+    x, rows = torch.randn(T, H, generator=g).to(t), torch.randn(T * k, H, generator=g).to(t)
+    rows[int(offsets[E]):] = float("nan")
+    w = torch.rand(T, k, generator=g)
+    at = lambda v, off=1: offset_copy(v.cuda(), off)
+    r = m.make_rows(T, H, E, k, t)
+    bits = {2: torch.int16, 4: torch.int32}[x.element_size()]
+    want = x.view(bits)[src.long().clamp(min=0)]
+    want[src < 0] = 0
+    for off in (1, 2, 4):
+        out = dispatched(r, idx.cuda(), at(x, off))
+        check_order(out, idx, E)
+        assert torch.equal(out["x_rows"].view(bits).cpu(), want), off
+    res, drows, dw = at(torch.zeros(T, H, dtype=t)), at(torch.zeros(T * k, H, dtype=t)), new(T, k)
+    for extra in (x, None):
+        m.moe_combine(r, at(rows), perm.cuda(), w.cuda(), None if extra is None else at(extra), res)
+        ref, mag = B.combine(rows, perm, w, extra)
+        B.within(res.clone(), ref, B.store(t, ref) + (k + 2) * B.U * mag, "out")
+    m.moe_combine_backward(r, at(x), at(rows), perm.cuda(), offsets.cuda(), w.cuda(), drows, dw)
+    assert m.moe_get_last_error() == 0
+    ref, rw, mag = B.combine_backward(x, rows, perm, w)
+    B.within(drows.clone(), ref, B.store(t, ref) + B.U * ref.abs(), "drows")
+    B.within(dw, rw, (B.chain(H) + 2) * B.U * mag, "dw")
+
+
+@pytest.mark.parametrize("T,H,k", [(37, 1031, 3), (300, 250, 9), (700, 8192, 2), (700, 1031, 9), (5000, 250, 4)])
+@pytest.mark.parametrize("off", [1, 2, 4, 8])
+def test_misaligned_codes_in_every_unit(T, H, k, off):
+    # 8-bit rows in units of one to eight bytes, in one launch and in more
+    g, m, E, t = gen(T + H + off), G.lib(), 24, torch.float8_e4m3fn
+    idx = B.routing(T, E, k, g, 0.2)
+    src = B.order(idx, E)[3].long()
+    x = torch.randint(0, 255, (T, H), generator=g, dtype=torch.uint8)
+    scale = torch.rand(T, generator=g)
+    out = dispatched(m.make_rows(T, H, E, k, t), idx.cuda(), offset_copy(x.cuda(), off).view(t), scale.cuda())
+    assert m.moe_get_last_error() == 0
+    check_order(out, idx, E)
+    want, want_scale = x[src.clamp(min=0)], scale[src.clamp(min=0)]
+    want[src < 0], want_scale[src < 0] = 0, 0
+    assert torch.equal(out["x_rows"].view(torch.uint8).cpu(), want)
+    assert torch.equal(out["scale_rows"].cpu(), want_scale)

@@ -421,3 +421,41 @@ def test_gradient_of_one_cluster(T, H, dtype):
     for _ in range(10):
         again = backward(n, h, gamma, x, x)
         assert torch.equal(again[0], dx) and torch.equal(again[1], dg)
+
+
+@pytest.mark.parametrize("T,H", [(7, 250), (700, 250), (700, 1031), (7, 8192), (350, 8193), (3, 33000)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_misaligned_buffers_in_every_variant(T, H, dtype):
+    # one value and eight a thread, several rows and one a block, rows read again for each pass
+    m, t = G.lib(), B.DTYPES[dtype]
+    x, r, gamma = inputs(T, H, t, True, seed=10)
+
+    def at(v):
+        flat = torch.empty(v.numel() + 1, dtype=v.dtype, device="cuda")
+        flat[1:].copy_(v.reshape(-1))
+        return flat[1:].view(v.shape)
+
+    n = m.make_norm(T, H, t)
+    out = [at(torch.zeros(T, H, dtype=t)) for _ in range(2)] + [
+        at(torch.zeros(T, H, dtype=torch.uint8)).view(E4M3), new(T)]
+    m.moe_add_rmsnorm(n, at(x), at(r), at(gamma), *out)
+    check_forward([out[0].clone(), out[1].clone(), out[2].view(torch.uint8).clone().view(E4M3), out[3]], x, r, gamma)
+    ws = new(m.moe_norm_workspace_bytes(n), dtype=torch.uint8)
+    for dh in (x, None):
+        dx, dg = at(torch.zeros(T, H, dtype=t)), new(H)
+        m.moe_add_rmsnorm_backward(n, at(r), at(gamma), at(x), None if dh is None else at(dh), dx, dg, ws)
+        assert m.moe_get_last_error() == 0
+        check_backward(dx.clone(), dg, r, gamma, x, dh)
+
+
+@pytest.mark.parametrize("dtype,H", [("f32", 16387), ("f32", 16389), ("f32", 8193), ("bf16", 32771), ("f16", 32777),
+                                     ("bf16", 16387), ("f16", 12289)])
+@pytest.mark.parametrize("T", [2, 200])
+def test_widest_shifted_rows(dtype, H, T):
+    # the last widths in registers and the first that are read again, forward and backward
+    m, t = G.lib(), B.DTYPES[dtype]
+    x, r, gamma = inputs(T, H, t, True, seed=11)
+    n = m.make_norm(T, H, t)
+    check_forward(forward(n, x, r, gamma), x, r, gamma)
+    dx, dg = backward(n, r, gamma, x, x)
+    check_backward(dx, dg, r, gamma, x, x)
