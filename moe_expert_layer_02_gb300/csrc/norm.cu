@@ -635,12 +635,13 @@ cudaError_t launch_add_rmsnorm(const void* x, const void* r, const void* gamma, 
                            static_cast<const E*>(gamma), static_cast<E*>(h), static_cast<E*>(y),
                            static_cast<uint8_t*>(q), q_scale, T, H, tpr, eps);
     };
-    // few rows: one vector a thread, for the shortest way through a row (64 rows of
-    // 8192 bf16 3.4 us, 4.2 with four; 304 rows 5.2 and 5.1; 608 rows 11.9 and 9.3)
-    if (n <= 1024 && T <= 2 * device_sm_count()) {
-      const int tpr = round32(n);
-      return go(add_rmsnorm_kernel<E, V, 1, 1024, kShift>, tpr, tpr);
-    }
+    // few rows: one vector a thread, for the shortest way through a row, while a
+    // multiprocessor's 1024 of them hold all rows (8192 bf16 with codes, against four: 64
+    // rows 3.5 and 4.1 us, 152 rows 3.7 and 4.3, 160 rows 5.4 and 4.7, 304 rows 5.4 and 5.1,
+    // 608 rows 12.3 and 9.7; 304 x 2880 2.9 and 4.0)
+    const int one = round32(n), sms = device_sm_count();
+    if (n <= 1024 && T <= 2 * sms && T * one <= 1024 * sms)
+      return go(add_rmsnorm_kernel<E, V, 1, 1024, kShift>, one, one);
     const int tpr = round32((n + kMany - 1) / kMany);
     if (tpr <= 256) return go(add_rmsnorm_kernel<E, V, kMany, 256, kShift>, 256, tpr);
     if (tpr <= 1024) return go(add_rmsnorm_kernel<E, V, kMany, 1024, kShift>, tpr, tpr);
