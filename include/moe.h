@@ -354,11 +354,18 @@ int moe_forward(const moe_problem* p, const void* x, const float* router_w,
  * experts and back in the caller's own type, and the gradients, for programs
  * that run (or train) experts of their own or put the layer's steps together
  * themselves.  Conventions are those above, except that widths need not be
- * multiples of 128 and that pointers need only their elements' alignment (buffers
- * that start on 16-byte boundaries are read and written in 16-byte vectors, whatever
- * the width; others one element at a time); calls that need scratch name their own
- * size function.  Every sum is taken in fp32 in a fixed order and rounded
- * once: results repeat bit for bit.  Empty calls (T = 0) take NULL tensors.
+ * multiples of 128 and that pointers need only their elements' alignment; calls that
+ * need scratch name their own size function.  Every sum is taken in fp32 in a fixed
+ * order and rounded once: results repeat bit for bit.  Empty calls (T = 0) take NULL
+ * tensors.
+ * How rows are read and written matters for speed alone: in 16-byte vectors where the
+ * buffers start on 16-byte boundaries, one element at a time where they do not.  Rows
+ * of no whole number of vectors go
+ *   - in moe_dispatch by the widest unit of 1 to 8 bytes that divides a row, with up to
+ *     2048 slots or rows of whole 8-byte units; in vectors otherwise (off 16-byte
+ *     boundaries always by the widest unit that divides rows and addresses)
+ *   - in moe_add_rmsnorm by elements past 32768 values (16384 in fp32), in its gradient
+ *     past about 16384 (8192); in vectors otherwise, as in all other calls
  * ------------------------------------------------------------------------ */
 
 /* Element type of token rows. */

@@ -13,7 +13,7 @@
 // The norm is taken from the fp32 sum x + r, so y and q are rounded once, from
 // that; the stored h is its rounding to the caller's type.  Both passes are bound by
 // memory; on GB300, against the 6764 GB/s of a plain copy, 16384 x 8192 bf16 with
-// residual and fp8 rows takes 177 us (6.8 TB/s), the gradient of 8192 x 7168 bf16
+// residual and fp8 rows takes 178 us (6.8 TB/s), the gradient of 8192 x 7168 bf16
 // 74 us (6.4 TB/s; its second kernel, the sum of the blocks' dgamma, 3 of them).
 #include <algorithm>
 
